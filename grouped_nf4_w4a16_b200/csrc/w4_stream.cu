@@ -542,8 +542,10 @@ __device__ __forceinline__ void stage_rows(const StreamParams &a, Shared &sh, co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int k0 = c * a.chunk, n8 = min(a.chunk, a.K - k0) / 8;
   const int parts = nrows < kWarps ? kWarps / nrows : 1, step = parts * 32;
-  uint32_t *rowmax = sh.rowmax[turn & 1];   // zero; the next turn's is cleared here
-  if (parts > 1 && tid < kWarps) sh.rowmax[(turn & 1) ^ 1][tid] = 0u;
+  // Zero; the next turn's is cleared here, also in turns that use neither: what the turn before
+  // left there (read before that turn's last barrier) would scale the next turn's rows.
+  uint32_t *rowmax = sh.rowmax[turn & 1];
+  if (tid < kWarps) sh.rowmax[(turn & 1) ^ 1][tid] = 0u;
   // (with several warps to a row every warp goes round once, for the barrier)
 #pragma unroll 1
   for (int task = warp; parts > 1 ? task == warp : task < nrows; task += kWarps) {
