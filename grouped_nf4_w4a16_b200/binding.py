@@ -467,6 +467,15 @@ def _shape(t: torch.Tensor, name: str, shape: tuple):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _scratch(workspace: Optional[torch.Tensor], nbytes, device) -> torch.Tensor:
+    """The caller's workspace, one run of as many bytes as it counts, or a fresh one of nbytes()."""
+    if workspace is None:
+        return make_workspace(nbytes(), device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
 def gnf4_moe_route(hidden: torch.Tensor, router_w: torch.Tensor, top_k: int, *,
                    bias: Optional[torch.Tensor] = None, renormalize: bool = True, logits=None,
                    topk_ids=None, topk_weights=None, workspace: Optional[torch.Tensor] = None,
@@ -499,8 +508,7 @@ def gnf4_moe_route(hidden: torch.Tensor, router_w: torch.Tensor, top_k: int, *,
             _shape(t, name, (T, n))
         outs.append(t)
     topk_ids, topk_weights, logits = outs
-    if workspace is None:
-        workspace = make_workspace(gnf4_workspace_bytes(GNF4_OP_MOE_ROUTE, T), dev)
+    workspace = _scratch(workspace, lambda: gnf4_workspace_bytes(GNF4_OP_MOE_ROUTE, T), dev)
     st = load_library().gnf4_moe_route(
         hidden.data_ptr(), router_w.data_ptr(), _ptr(bias), T, H, E, top_k, 1 if renormalize else 0,
         logits.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), workspace.data_ptr(),
@@ -551,9 +559,8 @@ def gnf4_moe_experts(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights:
     else:
         _need(out, "out", torch.bfloat16)
         _shape(out, "out", (T, H))
-    if workspace is None:
-        workspace = make_workspace(gnf4_workspace_bytes(GNF4_OP_MOE_EXPERTS, T * k, F2, H, E),
-                                   hidden.device)
+    workspace = _scratch(
+        workspace, lambda: gnf4_workspace_bytes(GNF4_OP_MOE_EXPERTS, T * k, F2, H, E), hidden.device)
     d = ExpertsDesc(_EXPERTS_DESC_BYTES, fmt, sdt, epilogue, swiglu_alpha, swiglu_limit, k, H, F, E,
                     T, hidden.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(),
                     w_gate_up.data_ptr(), s_gate_up.data_ptr(), w_down.data_ptr(),
@@ -609,8 +616,7 @@ def gnf4_gemv(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, *, fmt: in
     else:
         ldy = _rows(y, "y", N)
         _shape(y, "y", (M, N))
-    if workspace is None:
-        workspace = make_workspace(gnf4_workspace_bytes(GNF4_OP_GEMV, M, N, K), x.device)
+    workspace = _scratch(workspace, lambda: gnf4_workspace_bytes(GNF4_OP_GEMV, M, N, K), x.device)
     d = GemvDesc(_GEMV_DESC_BYTES, fmt, sdt, K // scales.shape[1], M, N, K, ldx, ldy, x.data_ptr(),
                  w.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(bias), y.data_ptr())
     st = load_library().gnf4_gemv(d, workspace.data_ptr(), workspace.nbytes, raw)

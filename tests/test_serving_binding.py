@@ -1,0 +1,37 @@
+"""The binding's own checks of gnf4_moe_route, gnf4_moe_experts and gnf4_gemv, which come before
+the library sees a pointer (no GPU: host tensors pass as device ones up to the library)."""
+import pytest
+import torch
+
+import grouped_nf4_w4a16_b200 as gnf4
+from grouped_nf4_w4a16_b200 import binding
+
+
+@pytest.fixture
+def as_if_on_device(monkeypatch):
+    monkeypatch.setattr(binding, "_here", lambda t, where: 0)
+
+
+def calls(**kw):
+    bf = torch.zeros((2, 64), dtype=torch.bfloat16)
+    w = torch.zeros((128, 32), dtype=torch.uint8)
+    s = torch.zeros((128, 1))
+    ids = torch.zeros((2, 1), dtype=torch.int32)
+    return [
+        lambda: gnf4.gnf4_moe_route(bf, bf, 1, **kw),
+        lambda: gnf4.gnf4_moe_experts(bf, ids, torch.zeros((2, 1)), w[None], s[None], w[None, :64],
+                                      s[None, :64], **kw),
+        lambda: gnf4.gnf4_gemv(bf, w, s, **kw),
+    ]
+
+
+@pytest.mark.parametrize("call", range(3))
+def test_workspaces_that_count_more_bytes_than_they_hold(as_if_on_device, call):
+    one = torch.zeros(1, dtype=torch.uint8)
+    # a byte shown 2^30 times; every other byte of a buffer
+    for workspace in (one.expand(1 << 30), torch.zeros(1 << 24, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            calls(workspace=workspace)[call]()
+    # an ordinary one gets as far as the library, which knows host memory
+    with pytest.raises(gnf4.Gnf4Error, match="HOST_POINTER"):
+        calls(workspace=torch.zeros(1 << 24, dtype=torch.uint8))[call]()
