@@ -440,6 +440,8 @@ def _here(t: torch.Tensor, where: str) -> Optional[int]:
 def _elsewhere(fn, t: torch.Tensor, stream, args, kwargs):
     """fn on t's device and on `stream` (default: that device's current one): what fn allocates or
     zeroes is then ordered with the kernels it launches."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
     with torch.cuda.device(t.device):
         if stream is None:
             return fn(*args, **kwargs)

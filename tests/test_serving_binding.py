@@ -35,3 +35,34 @@ def test_workspaces_that_count_more_bytes_than_they_hold(as_if_on_device, call):
     # an ordinary one gets as far as the library, which knows host memory
     with pytest.raises(gnf4.Gnf4Error, match="HOST_POINTER"):
         calls(workspace=torch.zeros(1 << 24, dtype=torch.uint8))[call]()
+
+
+class FakeStream:
+    def __init__(self, device):
+        self.device = torch.device(device)
+
+
+class Nothing:
+    def __init__(self, *args, **kw):
+        pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *args):
+        return False
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """torch.cuda.stream(s) makes s's device current, so the call would have gone to the tensors'
+    device and its current stream."""
+    used = []
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "device", Nothing)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: used.append(s) or Nothing())
+    t = type("T", (), dict(device=torch.device("cuda:0")))()
+    ran = lambda: "ran"
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        binding._elsewhere(ran, t, FakeStream("cuda:1"), (), {})
+    own = FakeStream("cuda:0")
+    assert binding._elsewhere(ran, t, own, (), {}) == "ran" and used == [own]
