@@ -446,8 +446,8 @@ def _elsewhere(fn, t: torch.Tensor, stream, args, kwargs):
         if stream is None:
             return fn(*args, **kwargs)
         if not isinstance(stream, torch.cuda.Stream):
-            # (handle 0, the legacy default stream, is torch's default stream)
-            stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
+            # (CUDA's handles 0 and 1, the legacy default stream, are torch's default stream)
+            stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream) > 1
                       else torch.cuda.default_stream(t.device))
         with torch.cuda.stream(stream):
             return fn(*args, **kwargs)

@@ -66,3 +66,16 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
         binding._elsewhere(ran, t, FakeStream("cuda:1"), (), {})
     own = FakeStream("cuda:0")
     assert binding._elsewhere(ran, t, own, (), {}) == "ran" and used == [own]
+
+
+@pytest.mark.parametrize("handle,kind", [(0, "default"), (1, "default"), (2, 2), (0x7f00, 0x7f00)])
+def test_stream_handles(monkeypatch, handle, kind):
+    """Handles 0 and 1 are the legacy default stream (1 is no address an ExternalStream can hold)."""
+    used = []
+    monkeypatch.setattr(torch.cuda, "device", Nothing)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: used.append(s) or Nothing())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device: h)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: "default")
+    t = type("T", (), dict(device=torch.device("cuda:0")))()
+    binding._elsewhere(lambda: None, t, handle, (), {})
+    assert used == [kind]
