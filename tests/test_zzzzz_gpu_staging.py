@@ -7,8 +7,9 @@ import pytest
 import torch
 
 import grouped_nf4_w4a16_b200 as gnf4
-from test_w4_stream_staging import ALTERNATING, alternating
-from test_zzzz_gpu_serving import FMT, gen, packed
+from test_w4_stream_staging import ALTERNATING, LAYERS_IN_CHUNKS, PRODUCTS_IN_CHUNKS, alternating
+from test_zzzz_gpu_serving import (FMT, close, experts_case, experts_ref, gemv_case, gemv_ref, gen, packed,
+                                   run_experts)
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,44 @@ def test_no_token_scales_another_one(case):
             out = gnf4.gnf4_moe_experts(large, ids, share, *weights, fmt=FMT[fmt])
             others = torch.arange(T, device="cuda") != t
             assert torch.equal(out[others], clean[others]), (t, factor)
+
+
+@pytest.mark.parametrize("layer,up,down,shared", LAYERS_IN_CHUNKS)
+def test_layers_in_chunks_against_fp64(layer, up, down, shared):
+    T, H, F, E, k, fmt, scale, inter = layer
+    case = experts_case(T + H + F, T, H, F, E, k, fmt, scale)
+    close(run_experts(case, fmt, inter), *experts_ref(*case, fmt, inter))
+
+
+@pytest.mark.parametrize("product,chunks,shared", PRODUCTS_IN_CHUNKS)
+def test_vector_products_in_chunks_against_fp64(product, chunks, shared):
+    M, N, K, fmt, group, scale, zeros = product
+    x, w, s, z, b = gemv_case(M + N + K, M, N, K, fmt, group, scale, zeros, True)
+    close(gnf4.gnf4_gemv(x, w, s, fmt=FMT[fmt], zeros=z, bias=b), *gemv_ref(x, w, s, z, b, fmt, group))
+
+
+def test_zero_points_up_to_255():
+    x, w, s, z, _ = gemv_case(3, 9, 100, 512, "int4", 64, "f32", True)
+    z = torch.randint(0, 256, z.shape, generator=gen(8), device="cuda", dtype=torch.uint8)
+    close(gnf4.gnf4_gemv(x, w, s, fmt=FMT["int4"], zeros=z), *gemv_ref(x, w, s, z, None, "int4", 64))
+
+
+@pytest.mark.parametrize("layer,up,down,shared", LAYERS_IN_CHUNKS)
+def test_a_special_token_reaches_no_other_in_chunks(layer, up, down, shared):
+    """Each token in turn with a NaN, an infinity or everything 2^40 larger: the others keep their bits."""
+    T, H, F, E, k, fmt, scale, inter = layer
+    case = list(experts_case(T + H + F, T, H, F, E, k, fmt, scale))
+    hidden, clean = case[0], run_experts(case, fmt, inter)
+    for t in range(T):
+        for what in range(3):
+            case[0] = hidden.clone()
+            if what == 0:
+                case[0][t, 7 * t % H] = math.nan
+            elif what == 1:
+                case[0][t, 11 * t % H] = math.inf
+            else:
+                case[0][t] *= 2.0 ** 40
+            out = run_experts(case, fmt, inter)
+            others = torch.arange(T, device="cuda") != t
+            assert torch.equal(out[others], clean[others]), (t, what)
+            assert what != 0 or torch.isnan(out[t].float()).all()
