@@ -469,6 +469,13 @@ def _shape(t: torch.Tensor, name: str, shape: tuple):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _fit(where: str, *sizes: int):
+    """Sizes that a C int32 holds (the library checks the rest)."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            raise Gnf4Error(3, where)
+
+
 def _scratch(workspace: Optional[torch.Tensor], nbytes, device) -> torch.Tensor:
     """The caller's workspace, one run of as many bytes as it counts, or a fresh one of nbytes()."""
     if workspace is None:
@@ -495,6 +502,7 @@ def gnf4_moe_route(hidden: torch.Tensor, router_w: torch.Tensor, top_k: int, *,
     T, H = hidden.shape
     E = router_w.shape[0]
     _shape(router_w, "router_w", (E, H))
+    _fit("gnf4_moe_route", H, E, top_k)
     dev = hidden.device
     if bias is not None:
         _need(bias, "bias", torch.float32)
@@ -549,6 +557,7 @@ def gnf4_moe_experts(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights:
     E, F2, _ = w_gate_up.shape
     F = F2 // 2
     block = 32 if fmt == GNF4_FMT_MXFP4 else 64
+    _fit("gnf4_moe_experts", k, H, F2, E)
     _shape(topk_ids, "topk_ids", (T, k))
     _shape(topk_weights, "topk_weights", (T, k))
     _shape(w_gate_up, "w_gate_up", (E, 2 * F, H // 2))
@@ -603,6 +612,7 @@ def gnf4_gemv(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, *, fmt: in
     M = x.shape[0]
     N, Kh = w.shape
     K = 2 * Kh
+    _fit("gnf4_gemv", M, N, K)
     ldx = _rows(x, "x", K)
     if scales.dim() != 2 or scales.shape[0] != N or scales.shape[1] < 1 or K % scales.shape[1]:
         raise ValueError(f"scales must be [{N}, {K}/group], got {list(scales.shape)}")

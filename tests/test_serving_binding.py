@@ -79,3 +79,38 @@ def test_stream_handles(monkeypatch, handle, kind):
     t = type("T", (), dict(device=torch.device("cuda:0")))()
     binding._elsewhere(lambda: None, t, handle, (), {})
     assert used == [kind]
+
+
+BEYOND = 1 << 32
+
+
+def meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("call", [
+    lambda: gnf4.gnf4_moe_route(meta(1, BEYOND + 64), meta(2, BEYOND + 64), 1),
+    lambda: gnf4.gnf4_moe_route(meta(1, 64), meta(BEYOND + 4, 64), 1),
+    lambda: gnf4.gnf4_moe_route(meta(1, 64), meta(4, 64), BEYOND + 1),
+    lambda: gnf4.gnf4_moe_route(meta(1, 64), meta(4, 64), 2 - BEYOND),
+    lambda: gnf4.gnf4_moe_experts(
+        meta(1, 64), meta(1, BEYOND + 1, dtype=torch.int32), meta(1, BEYOND + 1, dtype=torch.float32),
+        meta(2, 128, 32, dtype=torch.uint8), meta(2, 128, 1, dtype=torch.float32),
+        meta(2, 64, 32, dtype=torch.uint8), meta(2, 64, 1, dtype=torch.float32)),
+    lambda: gnf4.gnf4_moe_experts(
+        meta(1, 64), meta(1, 1, dtype=torch.int32), meta(1, 1, dtype=torch.float32),
+        meta(BEYOND + 2, 128, 32, dtype=torch.uint8), meta(BEYOND + 2, 128, 1, dtype=torch.float32),
+        meta(BEYOND + 2, 64, 32, dtype=torch.uint8), meta(BEYOND + 2, 64, 1, dtype=torch.float32)),
+    lambda: gnf4.gnf4_moe_experts(
+        meta(1, 64), meta(1, 1, dtype=torch.int32), meta(1, 1, dtype=torch.float32),
+        meta(2, 2 * (BEYOND + 64), 32, dtype=torch.uint8), meta(2, 2 * (BEYOND + 64), 1, dtype=torch.float32),
+        meta(2, 64, (BEYOND + 64) // 2, dtype=torch.uint8), meta(2, 64, (BEYOND + 64) // 64, dtype=torch.float32)),
+    lambda: gnf4.gnf4_gemv(meta(1, 64), meta(BEYOND + 5, 32, dtype=torch.uint8), meta(BEYOND + 5, 1, dtype=torch.float32)),
+    lambda: gnf4.gnf4_gemv(meta(1, BEYOND + 64), meta(5, (BEYOND + 64) // 2, dtype=torch.uint8),
+                           meta(5, (BEYOND + 64) // 64, dtype=torch.float32)),
+    lambda: gnf4.gnf4_gemv(meta(BEYOND + 1, 64), meta(5, 32, dtype=torch.uint8), meta(5, 1, dtype=torch.float32)),
+])
+def test_sizes_beyond_32_bits_are_refused(as_if_on_device, call):
+    """They do not fit the C fields, where their low 32 bits would look like an ordinary size."""
+    with pytest.raises(gnf4.Gnf4Error, match="UNSUPPORTED_SHAPE"):
+        call()
