@@ -81,3 +81,32 @@ def test_a_special_token_reaches_no_other_in_chunks(layer, up, down, shared):
             others = torch.arange(T, device="cuda") != t
             assert torch.equal(out[others], clean[others]), (t, what)
             assert what != 0 or torch.isnan(out[t].float()).all()
+
+
+def test_gemv_small_scales():
+    """Scales enter times 2^-14: exactly from 2^-112 on, below as multiples of 2^-135 (half a step
+    is 2^-136). Sums are fp32 of rows with a largest magnitude below 2: each of the K / 64 additions
+    is off by up to 2^-150 there, times the row's largest magnitude in the result."""
+    x, w, _, _, _ = gemv_case(12, 4, 60, 512, "nf4", 64, "f32")
+    x = (x.float() * 2.0 ** 90).to(torch.bfloat16)
+    top = x.double().abs().amax(1, keepdim=True)
+    step = torch.exp2(-torch.arange(100, 127, device="cuda").double())       # 2^-100 to 2^-126
+    s = (torch.rand((60, 8), generator=gen(6), device="cuda").double() + 1) * step[torch.arange(60, device="cuda") % 27, None]
+    s = s.float()
+    ref, err = gemv_ref(x, w, s, None, None, "nf4", 64)
+    total = x.double().abs() @ torch.ones((512, 60), dtype=torch.float64, device="cuda")
+    below = (s < 2.0 ** -112).any(1)
+    err = err + torch.where(below, 2.0 ** -136 * total, torch.zeros_like(total)) + 8 * 2.0 ** -150 * top
+    assert below.any() and not below.all()
+    close(gnf4.gnf4_gemv(x, w, s), ref, err)
+
+
+@pytest.mark.parametrize("T,k", [(1, 4), (3, 5), (8, 4), (2, 16)])
+def test_few_slots_with_an_expert_named_often(T, k):
+    """Up to 32 slots, more of one expert than a batch has rows: the general tables."""
+    case = list(experts_case(T + k, T, 192, 128, 6, k, "nf4", "f32", distinct=False))
+    case[1][:] = 4
+    case[1][0, 0] = -1
+    close(run_experts(case, "nf4", False), *experts_ref(*case, "nf4", False))
+    case[1][T - 1, k - 1] = 1
+    close(run_experts(case, "nf4", False), *experts_ref(*case, "nf4", False))
