@@ -469,17 +469,11 @@ def _shape(t: torch.Tensor, name: str, shape: tuple):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _fit(where: str, *sizes: int):
-    """Sizes that a C int32 holds (the library checks the rest)."""
-    for n in sizes:
-        if not -0x80000000 <= n <= 0x7FFFFFFF:
-            raise Gnf4Error(3, where)
+_INT32 = 0x7FFFFFFF   # sizes past it would lose their high bits on the way (the library checks the rest)
 
 
-def _scratch(workspace: Optional[torch.Tensor], nbytes, device) -> torch.Tensor:
-    """The caller's workspace, one run of as many bytes as it counts, or a fresh one of nbytes()."""
-    if workspace is None:
-        return make_workspace(nbytes(), device)
+def _whole(workspace: torch.Tensor) -> torch.Tensor:
+    """A caller's workspace: one run of as many bytes as it counts."""
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace
@@ -502,7 +496,8 @@ def gnf4_moe_route(hidden: torch.Tensor, router_w: torch.Tensor, top_k: int, *,
     T, H = hidden.shape
     E = router_w.shape[0]
     _shape(router_w, "router_w", (E, H))
-    _fit("gnf4_moe_route", H, E, top_k)
+    if H > _INT32 or E > _INT32 or abs(top_k) > _INT32:
+        raise Gnf4Error(3, "gnf4_moe_route")
     dev = hidden.device
     if bias is not None:
         _need(bias, "bias", torch.float32)
@@ -518,7 +513,8 @@ def gnf4_moe_route(hidden: torch.Tensor, router_w: torch.Tensor, top_k: int, *,
             _shape(t, name, (T, n))
         outs.append(t)
     topk_ids, topk_weights, logits = outs
-    workspace = _scratch(workspace, lambda: gnf4_workspace_bytes(GNF4_OP_MOE_ROUTE, T), dev)
+    workspace = (make_workspace(gnf4_workspace_bytes(GNF4_OP_MOE_ROUTE, T), dev) if workspace is None
+                 else _whole(workspace))
     st = load_library().gnf4_moe_route(
         hidden.data_ptr(), router_w.data_ptr(), _ptr(bias), T, H, E, top_k, 1 if renormalize else 0,
         logits.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), workspace.data_ptr(),
@@ -557,7 +553,8 @@ def gnf4_moe_experts(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights:
     E, F2, _ = w_gate_up.shape
     F = F2 // 2
     block = 32 if fmt == GNF4_FMT_MXFP4 else 64
-    _fit("gnf4_moe_experts", k, H, F2, E)
+    if k > _INT32 or H > _INT32 or F2 > _INT32 or E > _INT32:
+        raise Gnf4Error(3, "gnf4_moe_experts")
     _shape(topk_ids, "topk_ids", (T, k))
     _shape(topk_weights, "topk_weights", (T, k))
     _shape(w_gate_up, "w_gate_up", (E, 2 * F, H // 2))
@@ -570,8 +567,8 @@ def gnf4_moe_experts(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights:
     else:
         _need(out, "out", torch.bfloat16)
         _shape(out, "out", (T, H))
-    workspace = _scratch(
-        workspace, lambda: gnf4_workspace_bytes(GNF4_OP_MOE_EXPERTS, T * k, F2, H, E), hidden.device)
+    workspace = (make_workspace(gnf4_workspace_bytes(GNF4_OP_MOE_EXPERTS, T * k, F2, H, E), hidden.device)
+                 if workspace is None else _whole(workspace))
     d = ExpertsDesc(_EXPERTS_DESC_BYTES, fmt, sdt, epilogue, swiglu_alpha, swiglu_limit, k, H, F, E,
                     T, hidden.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(),
                     w_gate_up.data_ptr(), s_gate_up.data_ptr(), w_down.data_ptr(),
@@ -612,7 +609,8 @@ def gnf4_gemv(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, *, fmt: in
     M = x.shape[0]
     N, Kh = w.shape
     K = 2 * Kh
-    _fit("gnf4_gemv", M, N, K)
+    if M > _INT32 or N > _INT32 or K > _INT32:
+        raise Gnf4Error(3, "gnf4_gemv")
     ldx = _rows(x, "x", K)
     if scales.dim() != 2 or scales.shape[0] != N or scales.shape[1] < 1 or K % scales.shape[1]:
         raise ValueError(f"scales must be [{N}, {K}/group], got {list(scales.shape)}")
@@ -628,7 +626,8 @@ def gnf4_gemv(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, *, fmt: in
     else:
         ldy = _rows(y, "y", N)
         _shape(y, "y", (M, N))
-    workspace = _scratch(workspace, lambda: gnf4_workspace_bytes(GNF4_OP_GEMV, M, N, K), x.device)
+    workspace = (make_workspace(gnf4_workspace_bytes(GNF4_OP_GEMV, M, N, K), x.device)
+                 if workspace is None else _whole(workspace))
     d = GemvDesc(_GEMV_DESC_BYTES, fmt, sdt, K // scales.shape[1], M, N, K, ldx, ldy, x.data_ptr(),
                  w.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(bias), y.data_ptr())
     st = load_library().gnf4_gemv(d, workspace.data_ptr(), workspace.nbytes, raw)
