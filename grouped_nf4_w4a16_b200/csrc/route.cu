@@ -29,11 +29,18 @@
 //
 // The blocks of one token tile count themselves; the last one chooses.
 //
-// Measured on one B200: 4096 tokens x 8 experts, H 6144, 24 us (50 MB, 2.1
-// TB/s; 201 M multiply-adds fill the fp64 tensor pipe for 11 us of it, and the
-// MMA is what its warps wait for); one token x 64 experts, H 2048, 6.4 us; 64
-// tokens x 128 experts, H 2880, 7.3 us (latency: launch, two dependent loads,
-// the last block's choice).
+// Measured on one B200 (graph replays): 4096 tokens x 8 experts, H 6144, 22.8
+// us (50 MB, 2.2 TB/s; 201 M multiply-adds fill the fp64 tensor pipe for 11 us
+// of it, and the MMA is what its warps wait for); one token x 64 experts, H
+// 2048, 6.4 us; 64 tokens x 128 experts, H 2880, 7.1 us (latency: launch, two
+// dependent loads, the last block's choice).
+// Where T*H*E is large the fp64 pipe makes it slower than a bf16 product with
+// fp32 sums (a library GEMM) followed by gnf4_router_topk, whose choice then
+// depends on the order of those sums: 256 x 128, H 2880, 13.7 and 10.6 us; 4096
+// x 64, H 2048, 64.9 and 30.5; 4096 x 128, H 2880, 157 and 21.7; 512 x 512, H
+// 2048, 71.7 and 13.1. Up to 128 x 64 and 64 x 128, and with 8 experts up to
+// 4096 tokens, this launch is the faster one (6.8 and 12.2, 7.1 and 10.2, 22.9
+// and 26.2 us).
 #include <climits>
 
 #include "launch.h"
@@ -273,8 +280,9 @@ cudaError_t launch_moe_route(const uint16_t *hidden, const uint16_t *router_w, c
   uint32_t *counters =
       reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + kWsHeaderBytes);
   // Two token tiles to a block once they leave a block for every SM: the
-  // experts' side is converted once for both (4096 tokens, 8 experts,
-  // H 6144: 21.2 us against 25.7 with one; up to 256 tokens the same).
+  // experts' side is converted once for both. With two, in us, against one:
+  // 4096 x 8, H 6144, 22.9 and 28.4; 256 x 128, H 2880, 13.7 and 17.1; below
+  // the border 2048 x 8 16.6 and 15.9, 128 x 64, H 2048, 8.6 and 6.8.
   const int64_t tiles = (T + kTile - 1) / kTile, groups = (E + kTile - 1) / kTile;
   const bool two = tiles * groups >= 2 * device_sm_count();
   const int64_t blocks = (two ? (tiles + 1) / 2 : tiles) * groups;

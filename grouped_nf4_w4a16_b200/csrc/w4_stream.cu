@@ -19,6 +19,14 @@
 //   magnitude in [2^14, 2^15): exact for bf16 elements above 2^-28 of it. The
 //   activations between the two launches of gnf4_moe_experts stay fp32 in
 //   memory and are rounded to fp16 (2^-11 relative) on the same scale.
+//   What the roundings cost: against fp64 the experts' results are off by 1.62e-3
+//   to 1.69e-3 in relative norm, the exact ones rounded once to bf16 by 1 % less,
+//   the library's five launches (h and every slot's row in bf16) by 2.8e-3 to
+//   2.9e-3; a vector product's are off by its bf16 rounding to within 1e-6. One
+//   bf16 in ten (NF4 vector product: one in 25) falls to the other side of a
+//   rounding border than with fp32 throughout. So NF4 has one part for every
+//   row: the decode GEMM's second part for the up rows is half again as many
+//   table reads, in a kernel that is bound by them.
 //
 // Work split. Every warp streams its own share of W and meets the others only
 // where a share ends:
@@ -40,20 +48,21 @@
 // What bounds it (one B200, 6.55 TB/s copy bandwidth; figures of graph replays):
 //   MXFP4: issue slots. 85 warp instructions per 1024 codes, 67 % of the issue
 //     slots taken; an e2m1 conversion (two codes) runs once a clock and SM, 16
-//     of some 32 clocks. 64 tokens x 4 of 128 experts, 2880 x 2880: 346 us for
-//     1.47 GB, 4.2 TB/s; 4.7 in the stream itself.
+//     of some 32 clocks. 64 tokens x 4 of 128 experts, 2880 x 2880: 345 us for
+//     1.47 GB, 4.3 TB/s; 4.7 in the stream itself. (In runs of more than some
+//     50 ms the 1 kW power cap takes the SM clock from 1965 to 1820 MHz: 370 us.)
 //   NF4: shared memory. Per 1024 codes 16 wavefronts read the value table, 4
 //     the codes, 4 the copies write, and the activations; 73 % of the pipe's
-//     rate over the whole launch. 5 tokens x 2 of 8 experts, 6144 x 16384: 257
-//     us for the 1.0 to 1.2 GB of 6 or 7 experts, over 4 TB/s.
-//   16 rows, NF4, 32768 x 6144: 55.8 us for 114 MB: shared memory again (16 more
+//     rate over the whole launch. 5 tokens x 2 of 8 experts, 6144 x 16384: 256
+//     us for the 1.0 to 1.2 GB of 6 or 7 experts, over 4 TB/s (275 in long runs).
+//   16 rows, NF4, 32768 x 6144: 54.6 us for 114 MB: shared memory again (16 more
 //     wavefronts for the rows), and the rows are staged in two chunks of K.
 //   Small launches: latency. Of the 24 us of one token x 8 of 64 experts, NF4,
 //     2048 x 1024 (28 MB), each launch streams for 3 to 4; tables, staging and
 //     the end of the stream take 2 us each, most of it first passes through
 //     the code.
 //   INT4: the subtraction of zero points and the mantissa trick, 53 % of the
-//     ALU pipe; one row, 6144 x 16384, 22.7 us for 53 MB: 384 tiles on 148 SMs,
+//     ALU pipe; one row, 6144 x 16384, 22.1 us for 53 MB: 384 tiles on 148 SMs,
 //     so that a CTA has 2 tiles or 3.
 #include <algorithm>
 #include <climits>
@@ -1368,10 +1377,18 @@ int32_t chunk_of(int32_t K, int rows, int area) {
 // chunks, or its tiles leave many SMs a tile short. In microseconds: a CTA
 // reads a tile's 8 K bytes in K / 3750; a chunk in turn costs 5 (its staging,
 // the cut tiles, the ring's start); the join 2.5, and 1 for every 512 pieces of
-// 4 columns that a CTA may have to add up. (NF4, chunks in turn against split:
-// 16 rows 6144 x 16384 61.7 and 32.3 us, 2048 x 8192 29.4 and 15.1, 8192 x 4096
-// 20.4 and 16.3; 8 rows 4096 x 14336 34.4 and 19.0; 24 rows 32768 x 6144, which
-// the rule leaves in turn, 87 and 118 in a form with a slower join.)
+// 4 columns that a CTA may have to add up.
+// Chunks in turn and split, measured for NF4, MXFP4 and INT4 in groups of 128.
+// Split by the rule: 16 rows 6144 x 16384 64.1 and 34.9, 65.6 and 30.6, 54.8
+// and 31.8; 16 rows 2048 x 8192 30.6 and 16.3, 30.8 and 15.6, 24.0 and 15.7; 8
+// rows 4096 x 14336 32.3 and 20.3, 25.6 and 18.7, 27.2 and 19.1; 32 rows 2048 x
+// 8192 31.8 and 23.5, 31.8 and 23.0, 25.2 and 18.0. In turn by it: 1 row 6144 x
+// 16384 21.9 and 23.6, 19.1 and 20.2, 21.7 and 22.4; 1 row 2048 x 2048 7.0 and
+// 8.8, 7.5 and 9.1, 7.0 and 8.5; 32 rows 16384 x 4096 38.2 and 38.9, 37.0 and
+// 35.9, 31.0 and 36.3. Its constants are NF4's, and it misses some percent
+// where many tiles are joined: 16 rows 32768 x 6144 54.4 and 53.5, 51.0 and
+// 48.8, 50.4 and 47.9; 24 rows 86.8 and 85.9, 81.6 and 78.5, 83.4 and 80.0; 8
+// rows INT4 8192 x 8192 20.8 and 19.4.
 bool choose_split(StreamParams &p, int area) {
   if (p.N > kSplitColumns) return false;
   const int sms = device_sm_count();

@@ -47,7 +47,9 @@
 extern "C" {
 #endif
 
-#define GNF4_VERSION 120 /* 1.2.0: + gnf4_grouped_gemm_ex (MXFP4, bf16 absmax, gather, gpt-oss SwiGLU) */
+#define GNF4_VERSION 120 /* 1.2.0: + gnf4_grouped_gemm_ex (MXFP4, bf16 absmax, gather, gpt-oss SwiGLU).
+                            gnf4_moe_route, gnf4_moe_experts, gnf4_gemv and GNF4_FMT_INT4 were added
+                            under the same number: look for the symbols. */
 
 /* Exported entry points (the library is built with hidden default visibility). */
 #if defined(__GNUC__)
@@ -444,6 +446,11 @@ GNF4_API gnf4_status gnf4_moe_combine(const uint16_t *y, const int32_t *sorted_i
  *                 zero-filled once. gnf4_moe_route, gnf4_moe_experts and
  *                 gnf4_gemv may take turns on one workspace in stream order;
  *                 the library's other entry points may not share it.
+ * Meant for decode steps and for prompts over few experts. T * H * E fp64
+ * multiply-adds bound it: for prompts over many experts (above some 128 x 128
+ * tokens x experts) a library product with fp32 sums and gnf4_router_topk take
+ * less time (4096 x 128, H 2880: 157 us here, 22 there), at the price of a
+ * choice that depends on the order of the sums.
  * Alignment: bf16 tensors 2 bytes (with 16 and H % 8 == 0 they are read 16
  * bytes at a time), fp32 and int32 4, workspace 16.
  */
@@ -485,13 +492,19 @@ GNF4_API gnf4_status gnf4_moe_route(const uint16_t *hidden, const uint16_t *rout
  *   w_gate_up [E][2F][H/2], s_gate_up [E][2F][H/64 or H/32]
  *   w_down [E][H][F/2], s_down [E][H][F/64 or F/32]
  *   out [T][H] bf16 (written; must not overlap the inputs)
- * Numerics: code values as DECODE of gnf4_grouped_gemm (NF4 as one fp16 part
- *   within 6.0e-5, e2m1 exact); hidden in fp16 times a power of two per row
+ * There are no biases: a layer with a bias per expert on gate_up (before the
+ * activation) or on down has no argument for them here, nor in
+ * gnf4_grouped_gemm_ex.
+ * Numerics: NF4 code values as one fp16 part within 6.0e-5 in every row
+ *   (DECODE of gnf4_grouped_gemm keeps a remainder for the up rows of its
+ *   SwiGLU), e2m1 exact; hidden in fp16 times a power of two per row
  *   (exact above 2^-28 of the row's largest magnitude); h rounded to fp16 on
  *   the same kind of scale; every sum in fp32, of rows scaled to a largest
  *   magnitude of about 2 (so scales up to 2^108 in magnitude keep the sums
- *   inside fp32 where the result is). Results are the same from call to call
- *   on one GPU, and a NaN or infinity in one token reaches no other.
+ *   inside fp32 where the result is), with scales times 2^-14 (exact from
+ *   2^-112 on; smaller ones to the nearest multiple of 2^-135). Results are the
+ *   same from call to call on one GPU, and a NaN or infinity in one token
+ *   reaches no other.
  * Workspace: gnf4_workspace_bytes(GNF4_OP_MOE_EXPERTS, T * top_k, 2F, H, E, 1)
  *   bytes, zero-filled once (see gnf4_moe_route for sharing); it holds h and
  *   the slots' results. After GNF4_ERR_TIMEOUT zero it again. Word 2 of the
